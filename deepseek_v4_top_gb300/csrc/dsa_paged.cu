@@ -15,12 +15,19 @@
 //     W_j = 2^(x_j - m) with m a running reference of the head is the value
 //     weight itself; the softmax's denominator adds W_j / sigma_j in float32.
 //     Blocks of very different scales need no reference of their own.
-//   * W_j enters the value product as e4m3(W) + e5m2(W - e4m3(W)): at most
-//     2^-7 of W off (4 and 3 bits; 2^-9.6 on average, under the bf16 rounding
-//     of the output), or 2^-13 of the head's largest weight for small ones.
-//     A reference makes the first tile's largest weight 1 and moves only
-//     when one would pass 2^8 (e4m3 ends at 448): rare, and then O is rescaled
-//     in TMEM.
+//   * W_j enters the value product as e4m3(W) + e5m2(W - e4m3(W)): down to W =
+//     2^-6 at most 1.09 * 2^-8 of W off (4 and 3 bits; 2^-9.6 on average, under the
+//     bf16 rounding of the output), below that 1.07 * 2^-14.  The second adds up over
+//     a long tail of small weights, so the largest weight has to grow with the
+//     tiles: a reference makes the first tile's 5, and goes down an octave at
+//     tiles 5, 10, 20, 40 and 80 of a unit.  So t tiles never have less than a
+//     weight of t beside them, and lose at most 1.07 * 2^-7 of it (every 160th tile,
+//     heads whose largest weight there is below 160 go down to that).  A
+//     weight that would pass 2^8.75 (e4m3 ends at 448) moves the reference up.  A
+//     move rescales O in TMEM.  (With a largest weight of 1 at any length, one key 17
+//     octaves above 32767 flat ones lost a sixth of the output, and 2048 rows of 640
+//     keys took 256 us against 263 now; a first weight of 32 moves up in three tiles
+//     of four, not in one of eight: 302 us with moves down by each tile's maxima.)
 //
 // Split: the rows' 128-key tiles, row after row, are cut into one equal share
 // a CTA (each CTA finds its own share from the lengths on the device), so
@@ -113,13 +120,19 @@ __host__ __device__ constexpr uint32_t tmem_s(int buf) { return 128u * static_ca
 __host__ __device__ constexpr uint32_t tmem_o(int i) { return 256u + 64u * static_cast<uint32_t>(i); }
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kTop = 8.0f;                 // a weight above 2^kTop moves its head's reference,
-constexpr float kBase = 0.0f;                // which makes the tile's largest weight 2^kBase
+constexpr float kTop = 8.75f;                // a weight above 2^kTop moves its head's reference,
+constexpr float kBase = 2.3219281f;          // which makes the tile's largest weight 5 (a number that the terms hold),
+constexpr int kFirstDown = 5, kDowns = 5;    // times two after this tile of a unit and each doubling of it, so often;
+                                             // then (every 160 tiles) heads of lower weights go down to that,
+constexpr float kDown = 24.0f;               // but not further than this below their highest place
 
-// Flags of a tile: the first and the last of its unit, the last of the share.
+// Flags of a tile: the first and the last of its unit, the last of the share;
+// all references go down an octave, those of low weights are renewed; and, from
+// bit kLoweredShift on, how often they have gone down in the unit.
 // Of a unit: the last of the share, all tiles of its row, a row without a key,
 // a part that does not begin at the row's first tile.
-constexpr int kFirst = 1, kLast = 2, kEnd = 4, kWhole = 8, kEmpty = 16, kInside = 32;
+constexpr int kFirst = 1, kLast = 2, kEnd = 4, kWhole = 8, kEmpty = 16, kInside = 32, kLower = 64, kRenew = 128;
+constexpr int kLoweredShift = 8;
 constexpr int kUnits = 8;                    // units of which the index warp may be ahead of the output warps
 
 struct Misc {
@@ -142,7 +155,9 @@ struct Misc {
     uint64_t unit_full[kUnits]; // index warp -> output warps
     uint64_t drain;
     alignas(16) int red[3][64];          // by move: each head's largest x of the tile, in ordered_int's order
-    alignas(16) float refs[8][64];       // [softmax warp]: minus its heads' references, then the factors of the last move
+    // [softmax warp]: minus its heads' references; the factors of the last move; minus the lowest places that the
+    // references may take
+    alignas(16) float refs[8][96];
     alignas(16) float red_l[4][64];      // a finished unit's sums
     alignas(16) float m_ref[64];
     alignas(16) float fac[8][64];        // [output warp][head]: what the unit's value sums are multiplied by
@@ -328,8 +343,9 @@ __device__ void index_role(const PagedParams& p, Misc& ms, int lane) {
                 atomicOr(p.err, seq_bad ? DSA_DEVERR_SEQ_RANGE : DSA_DEVERR_NSEL_RANGE);
             }
         }
+        int left = kFirstDown, downs = 0;        // tiles until the references go down next, and how often they have
 #pragma unroll 1
-        for (int tt = t; tt < t1; ++tt, ++g) {
+        for (int tt = t; tt < t1; ++tt, ++g, --left) {
             // positions (-1: no key, -2: bad; a bad row has one bad key)
             int cur[4], page[4];
 #pragma unroll
@@ -359,6 +375,12 @@ __device__ void index_role(const PagedParams& p, Misc& ms, int lane) {
                     }
                 }
             }
+            int go = 0;
+            if (left == 0) {
+                go = downs < kDowns ? kLower : kRenew;
+                left = kFirstDown << downs;
+                downs += downs < kDowns ? 1 : 0;
+            }
             // a place without a usable key loads the row of the tile's first key (a
             // NaN there is the row's own), marked as its complement
             const int first = max(__shfl_sync(0xffffffffu, cur[0], 0), 0);
@@ -367,7 +389,8 @@ __device__ void index_role(const PagedParams& p, Misc& ms, int lane) {
             if (lane == 0)
                 *reinterpret_cast<int4*>(ms.tile[slot]) =
                     make_int4(n < 0 ? 1 : min(n - tt * 128, 128),
-                              (tt == t ? kFirst : 0) | (tt + 1 == t1 ? kLast | (last_unit ? kEnd : 0) : 0), 0, 0);
+                              (tt == t ? kFirst : 0) | (tt + 1 == t1 ? kLast | (last_unit ? kEnd : 0) : 0) | go | downs << kLoweredShift,
+                              0, 0);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&ms.ring_full[slot]));
         }
@@ -751,12 +774,16 @@ __device__ __forceinline__ void load_x(uint32_t ts, const float* qs, const float
 }
 
 // Moves the references of the heads whose largest weight over the tile's 128
-// keys passes 2^kTop (on a unit's first tile: all), so that it becomes
-// 2^kBase; the sums follow, and behind the first tile rescale_o() has to.  x is
-// used up.  red: this move's maxima, which were reset two moves ago.  Lane h
-// works out head h's move; the warp reads the factors back four at a time.
-__device__ __forceinline__ bool move_refs(const PagedParams& p, Misc& ms, int* red, int* red_reset, bool is_first, int g,
+// keys passes 2^kTop (on a unit's first tile: all), so that it becomes 2^base; on
+// a tile where `base` has grown by 1 the others go down by that, on one that
+// renews them those whose largest weight is below 2^base go down to it.  The sums
+// follow, and behind the first tile rescale_o() has to.  x is used up.  red: this
+// move's maxima, which were reset two moves ago.  Lane h works out head h's move;
+// the warp reads the factors back four at a time.
+__device__ __forceinline__ bool move_refs(const PagedParams& p, Misc& ms, int* red, int* red_reset, int flags, int g,
                                           uint32_t& ph_red, int h0, int lane, float* refs, float2* x, float2* l) {
+    const bool is_first = (flags & kFirst) != 0;
+    const float base = kBase + (flags >> kLoweredShift), grown = flags & kLower ? 1.0f : 0.0f;
     float v[32];
 #pragma unroll
     for (int h = 0; h < 16; ++h) {
@@ -769,10 +796,17 @@ __device__ __forceinline__ bool move_refs(const PagedParams& p, Misc& ms, int* r
     // (every warp has read the flag)
     if (!is_first && threadIdx.x == 0) *reinterpret_cast<volatile int*>(&ms.move[g & 1]) = 0;
     const float top = ordered_float(red[h0 + lane]);
-    // (a first tile without a finite score keeps reference 0)
-    const float by = top > (is_first ? -INFINITY : kTop) ? kBase - top : 0.0f;
-    refs[lane] += by;
-    refs[32 + lane] = ex2_approx_ftz(by);
+    // (a tile without a finite score leaves the reference, a first one 0)
+    const float was = refs[lane];
+    float now = was + grown;
+    if (is_first || top + grown > kTop) {
+        if (top > -INFINITY) now = was + (base - top);
+        refs[64 + lane] = is_first ? now + kDown : fminf(refs[64 + lane], now + kDown);
+    } else if ((flags & kRenew) != 0 && top < base && top > -INFINITY) {
+        now = fmaxf(was, fminf(was + (base - top), refs[64 + lane]));
+    }
+    refs[lane] = now;
+    refs[32 + lane] = ex2_approx_ftz(now - was);
     __syncwarp();
     if (!is_first) {
 #pragma unroll
@@ -860,15 +894,15 @@ __device__ void softmax_role(const PagedParams& p, uint8_t* smem, Misc& ms, uint
         float2 x[16];
         uint32_t hi[8], lo[8];
         // a pass with the references as they are; one for the maxima and
-        // another with moved references if a weight passed 2^kTop in any warp
-        // (a unit's first tile always takes its references from its maxima)
-        enum { kTry, kMove, kMoved } pass = flags & kFirst ? kMove : kTry;
+        // another with moved references if a weight passed 2^kTop in any warp (on a
+        // unit's first tile, and where references go down, always)
+        enum { kTry, kMove, kMoved } pass = flags & (kFirst | kLower | kRenew) ? kMove : kTry;
 #pragma unroll 1
         while (true) {
             load_x(ts, qs, refs, sig, lsig, x);
             if (pass == kMove) {
                 red = red == 2 ? 0 : red + 1;
-                if (!move_refs(p, ms, ms.red[red], ms.red[red == 0 ? 2 : red - 1], (flags & kFirst) != 0, g, ph_red, h0, lane, refs, x, l))
+                if (!move_refs(p, ms, ms.red[red], ms.red[red == 0 ? 2 : red - 1], flags, g, ph_red, h0, lane, refs, x, l))
                     return;
                 pass = kMoved;
                 continue;
@@ -884,7 +918,7 @@ __device__ void softmax_role(const PagedParams& p, uint8_t* smem, Misc& ms, uint
                 }
             }
             // weights, and their two 8-bit terms, by way of fp16 (11 bits of a
-            // weight up to 2^8, of which the terms keep 7)
+            // weight up to 2^8.75, of which the terms keep 7)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 uint32_t hw = 0, lw = 0;
@@ -916,7 +950,8 @@ __device__ void softmax_role(const PagedParams& p, uint8_t* smem, Misc& ms, uint
         for (int h = 0; h < 16; ++h) l[h] = fma2(x[h], both(inv), l[h]);
         // the last tile's value product has read P
         if (g > 0 && !paged_wait(smem_addr(&ms.pv_done), (g - 1) & 1, ab, p.err)) return;
-        if (pass == kMoved && !(flags & kFirst)) rescale_o(refs + 32, ts0);
+        if (pass == kMoved && !(flags & kFirst) && __any_sync(0xffffffffu, refs[32 + lane] != 1.0f))
+            rescale_o(refs + 32, ts0);
         *reinterpret_cast<uint4*>(prow + c0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(prow + (c0 ^ 16)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
         *reinterpret_cast<uint4*>(prow + kPPlane + c0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);

@@ -411,10 +411,12 @@ DSA_API dsa_status dsa_paged_append(const void* kv, const float* norm_weight, fl
  * gives zeros, whatever its q.
  *
  * Scores are sums of exact products of the stored codes and q, in float32;
- * the softmax is float32; the weights enter the value product in two 8-bit
- * terms: a weight is at most 2^-7 of itself off (2^-9.6 on average, under the
- * bf16 rounding of the output), or 2^-13 of the largest weight of its head
- * where that is more; the denominator has them in float32.  An element of q
+ * the softmax is float32; the weights e^{s_j} (times the key's scale) enter the
+ * value product in two 8-bit terms: a weight is at most 1.09 * 2^-8 of itself
+ * off (2^-9.6 on average, under the bf16 rounding of the output), but for
+ * weights far below their head's largest, which may be further off or left out:
+ * all they lose is at most 1.1 * 2^-7 of the sum of the row's weights, whatever
+ * the row's length.  The denominator has all of them in float32.  An element of q
  * below 2^-15 of its head's largest may be off by 2^-23 of that largest.  A q
  * element that is not finite makes its row and head NaN, and so does a NaN
  * code; a sink of NaN makes its head NaN, one of +inf zeros.  scale must be
