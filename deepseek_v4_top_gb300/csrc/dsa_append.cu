@@ -106,7 +106,18 @@ __device__ __forceinline__ double exact_inverse(const T* row, float eps, int lan
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const double m = sum * (1.0 / kD) + static_cast<double>(eps);
     const float mf = static_cast<float>(m);
-    if (!(mf > 1e-37f && mf < 1e38f)) return 1.0 / sqrt(m);
+    if (mf < kLeastMean) {
+        // squares may have underflowed
+        sum = 0.0;
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(x[a][i]), static_cast<double>(x[a][i]), sum);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        return 1.0 / sqrt(sum * (1.0 / kD) + static_cast<double>(eps));
+    }
+    if (!(mf < 1e38f)) return 1.0 / sqrt(m);
     // r (1 + e / 2 + 3 e^2 / 8) with e = 1 - m r^2 of about 2^-23: 2^-60 off
     const double r = __frsqrt_rn(mf), e = fma(-m * r, r, 1.0);
     return fma(r * e, fma(e, 0.375, 0.5), r);

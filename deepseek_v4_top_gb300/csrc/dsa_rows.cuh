@@ -67,7 +67,12 @@ __device__ __forceinline__ void store_row8(__nv_bfloat16* p, const float* x) {
 // order (four chains of four squares, two additions, five across the lanes:
 // 11 roundings of 2^-24); with eps, the root, the quotient and two products,
 // all correctly rounded, a value is at most 10 * 2^-24 off the 64-bit result.
-__device__ __forceinline__ void row_norm(float (&x)[2][8], const float (&w)[2][8], float eps) {
+// A mean that is so small that squares in it may have underflowed is taken
+// once more of 2^88 x, with 2^176 eps: the least element's square is then
+// normal, and y stays the same.
+constexpr float kLeastMean = 0x1p-100f;
+
+__device__ __forceinline__ float row_mean(const float (&x)[2][8], float eps) {
     float part[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -79,7 +84,19 @@ __device__ __forceinline__ void row_norm(float (&x)[2][8], const float (&w)[2][8
     float s = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float inv = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(s, 1.0f / kD, eps)));
+    return fmaf(s, 1.0f / kD, eps);
+}
+
+__device__ __forceinline__ void row_norm(float (&x)[2][8], const float (&w)[2][8], float eps) {
+    float m = row_mean(x, eps);
+    if (m < kLeastMean) {       // (the same in every lane)
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[a][i] *= 0x1p88f;
+        m = row_mean(x, eps * 0x1p88f * 0x1p88f);
+    }
+    const float inv = __fdiv_rn(1.0f, __fsqrt_rn(m));
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll

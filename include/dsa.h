@@ -329,7 +329,8 @@ DSA_API dsa_status dsa_topk_select(const float* scores, int ld, const int32_t* n
  * the rotation out (rope_table and positions are unused).  rope_dim is a
  * multiple of 32 up to 512.  Arithmetic is float32, with one rounding to
  * dtype at the end (a float32 sum of squares that overflows gives a row of
- * zeros).  q_out may be q and k_out may be k; otherwise outputs must not
+ * zeros; one of squares that underflow is taken of a scaled row).  With eps = 0
+ * a row of zeros gives NaN.  q_out may be q and k_out may be k; otherwise outputs must not
  * overlap inputs.  A position outside [0, n_positions) sets
  * DSA_DEVERR_POS_RANGE and that token's rows become NaN.
  * q, k, q_out, k_out, the weights and rope_table are 16-byte aligned device
