@@ -478,11 +478,12 @@ def _cache_args(cache, cache_scale, page_table, B, dev):
     return ac, asc, ap, n_pages, page_size, page_size // blocks, max_pages
 
 
-def dsa_paged_append(kv, row_offsets, seq_start, page_table, cache, cache_scale, norm_weight=None, eps=-1.0,
+def dsa_paged_append(kv, row_offsets, seq_start, page_table, cache, cache_scale, norm_weight=None, eps=None,
                      rope=None, rope_style=DSA_ROPE_PAIRS, stream=None):
     """Append latent rows kv [R,512] (float32 or bfloat16) to a paged 8-bit cache: rows
     [row_offsets[b], row_offsets[b+1]) are tokens seq_start[b], ... of sequence b (int32 [B+1], [B]),
-    normed (eps >= 0) and rotated (rope) as by dsa_qk_norm_rope, stored as e4m3 in cache
+    normed (eps >= 0; by default 1e-6 with a norm_weight, no norm without one) and rotated (rope) as by
+    dsa_qk_norm_rope, stored as e4m3 in cache
     [pages, page_size, 512] (uint8 or float8_e4m3fn) with a power-of-two scale for each block of
     scale_block tokens in cache_scale [pages, page_size / scale_block].  Returns (cache, cache_scale)."""
     f32, _, i32, rows, _, _ = _row_types()
@@ -495,6 +496,8 @@ def dsa_paged_append(kv, row_offsets, seq_start, page_table, cache, cache_scale,
     ac, asc, ap, n_pages, page_size, block, max_pages = _cache_args(cache, cache_scale, page_table, B, dev)
     at, n_pos, rope_dim = _rope_args(rope, f32, dev)
     w = _tensor("norm_weight", norm_weight, f32, (512,), dev) if norm_weight is not None else 0
+    if eps is None:
+        eps = 1e-6 if w else -1.0
     st = (_lib or load()).dsa_paged_append(ak, w, eps, at, n_pos, rope_dim, rope_style, ac, asc, ap, a_s, ao, R, B,
                                            n_pages, page_size, block, max_pages,
                                            DSA_F32 if kv.dtype in f32 else DSA_BF16, _stream_of(stream, dev))

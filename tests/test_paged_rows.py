@@ -87,3 +87,24 @@ def test_append_of_rows_whose_squares_underflow(S, f32, eps):
     want, wscale, _ = ref.append(x64, offsets, starts, pages, codes0, scales0, w, float(np.float32(eps)), table, 64, 0)
     assert np.array_equal(scale.cpu().numpy().astype(np.float64), wscale)
     assert np.array_equal(cache.cpu().numpy(), want)
+
+
+def test_append_takes_the_norm_with_its_weight():
+    """norm_weight without eps norms as dsa_qk_norm_rope does by default; neither leaves the rows as they are."""
+    import torch
+    from deepseek_v4_top_gb300 import dsa
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kv = torch.randn((5, 512), generator=g, device="cuda") * 3
+    w = 1 + 0.2 * torch.randn(512, generator=g, device="cuda")
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def stored(**kw):
+        cache, scale = torch.zeros((1, 16, 512), dtype=torch.uint8, device="cuda"), torch.ones((1, 16), device="cuda")
+        dsa.dsa_paged_append(kv, i32(0, 5), i32(0), i32(0).view(1, 1), cache, scale, **kw)
+        return torch.cat((cache.view(-1).float(), scale.view(-1)))
+
+    assert torch.equal(stored(norm_weight=w), stored(norm_weight=w, eps=1e-6))
+    assert not torch.equal(stored(norm_weight=w), stored())
+    assert torch.equal(stored(), stored(eps=-1.0)) and torch.equal(stored(eps=-1.0), stored(norm_weight=w, eps=-1.0))
+    assert torch.equal(stored(eps=1e-6), stored(norm_weight=torch.ones_like(w)))
+    assert dsa.dsa_get_device_error() == 0
