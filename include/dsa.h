@@ -386,7 +386,9 @@ DSA_API dsa_status dsa_qk_norm_rope(const void* q, const void* k, const float* q
  * full before it is shared).  Repeating a call stores the same codes again.
  * Device errors: row_offsets that decrease or leave [0, R], or a sequence
  * that would leave its page table's max_pages, set DSA_DEVERR_SEQ_RANGE and
- * append nothing of that sequence; a page outside [0, n_pages) sets
+ * append nothing of that sequence (offsets of that kind may also keep tokens of
+ * the call's other sequences from being stored, whole scale blocks of them);
+ * a page outside [0, n_pages) sets
  * DSA_DEVERR_PAGE_RANGE and its tokens are not stored; a position at or above
  * n_positions sets DSA_DEVERR_POS_RANGE and that row is stored as NaN.
  * kv, norm_weight and rope_table 16-byte aligned.  Host errors as

@@ -108,3 +108,46 @@ def test_append_takes_the_norm_with_its_weight():
     assert torch.equal(stored(), stored(eps=-1.0)) and torch.equal(stored(eps=-1.0), stored(norm_weight=w, eps=-1.0))
     assert torch.equal(stored(eps=1e-6), stored(norm_weight=torch.ones_like(w)))
     assert dsa.dsa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("offsets,bad,good", [
+    ([0, 1000, 8, 24], [1], [0, 1000, 1008, 1024]), ([0, 40, 5000, 60], [1, 2], [0, 40, 50, 60]),
+    ([0, -7, 90, 200], [0, 1], [0, 50, 90, 200])])
+def test_append_with_a_bad_offset_among_good_sequences(offsets, bad, good):
+    """Tokens of the good sequences may be missing, whole scale blocks of them; what is stored is right, nothing else
+    is touched, and the call with the right offsets then stores everything."""
+    from deepseek_v4_top_gb300 import dsa
+    rng = np.random.default_rng(29)
+    P, S, R, most = 32, 16, 1024, 40
+    B = len(offsets) - 1
+    kv = rng.standard_normal((R, 512)).astype(np.float32)
+    starts = np.array([3, 5, 0], np.int32)
+    pages = rng.permutation(B * most).reshape(B, most).astype(np.int32)
+    codes0 = ref.encode(rng.standard_normal((B * most, P, 512)) * 50)
+    scales0 = np.full((B * most, P // S), 2.0 ** -7, np.float32)
+    cache, scale = _dev(codes0), _dev(scales0)
+
+    def call(offs):
+        dsa.dsa_paged_append(_dev(kv), _dev(np.array(offs, np.int32)), _dev(starts), _dev(pages), cache, scale)
+        return dsa.dsa_get_device_error(), cache.cpu().numpy(), scale.cpu().numpy().astype(np.float64)
+
+    code, codes, scales = call(offsets)
+    assert code == dsa.DSA_DEVERR_SEQ_RANGE
+    left = codes0.copy(), scales0.astype(np.float64)
+    for b in range(B):
+        if b in bad:
+            assert np.array_equal(codes[pages[b]], left[0][pages[b]]) and np.array_equal(scales[pages[b]], left[1][pages[b]])
+            continue
+        n = offsets[b + 1] - offsets[b]
+        one = ref.append(kv.astype(np.float64)[offsets[b]:offsets[b + 1]], [0, n], starts[b:b + 1], pages[b:b + 1], codes0, scales0,
+                         None, -1.0, None, 0, 0)
+        for at in range(0, P * most, S):
+            page, place = pages[b, at // P], at % P
+            got = codes[page, place:place + S], scales[page, place // S]
+            new = one[0][page, place:place + S], one[1][page, place // S]
+            old = left[0][page, place:place + S], left[1][page, place // S]
+            assert any(np.array_equal(got[0], w[0]) and got[1] == w[1] for w in (new, old)), (b, at)
+    code, codes, scales = call(good)
+    assert code == 0
+    want, wscale, _ = ref.append(kv.astype(np.float64), good, starts, pages, codes0, scales0, None, -1.0, None, 0, 0)
+    assert np.array_equal(codes, want) and np.array_equal(scales, wscale)
