@@ -981,13 +981,34 @@ __device__ void softmax_role(const PagedParams& p, uint8_t* smem, Misc& ms, uint
 
 // ------------------------------------------------------------ output warps
 // 1 / (l + 2^(s2 - m)) of a head: what its value sum (relative to 2^m) is
-// multiplied by.  A head without keys and sink gives 0.
+// multiplied by.  A head without keys and sink gives 0.  Far below the sink the
+// value sum may be large enough for a result where the factor is below float32's
+// numbers: then -2^64 times the factor is returned, and the value sum takes
+// kDeep = -2^-64 first.
+constexpr float kDeep = -0x1p-64f;
+
 __device__ __forceinline__ float out_factor(float m, float l, const float* sink, int h) {
     const float s2 = sink ? __ldg(sink + h) * kLog2e : -INFINITY;
     if (s2 == -INFINITY && l == 0.0f) return 0.0f;
     const float ms = isfinite(s2) ? fmaxf(m, s2) : m;
     const float e1 = ex2_approx_ftz(m - ms), e2 = ex2_approx_ftz(s2 - ms);
-    return e1 / fmaf(l, e1, e2);
+    return (m - ms < -64.0f ? -ex2_approx_ftz(m - ms + 64.0f) : e1) / fmaf(l, e1, e2);
+}
+
+// Value sums of the heads far below their sink (those of negative factors) times
+// kDeep, where the output warp will read them: rare, and so apart from its loop.
+__device__ __noinline__ void deepen(const float* fac, uint32_t to, int h0, int H) {
+#pragma unroll 1
+    for (; h0 < H; h0 += 32) {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            float o[16];
+            tmem_ld16(to + tmem_o(i) + h0, o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] *= fac[h0 + j] < 0.0f ? kDeep : 1.0f;
+            tmem_st16(to + tmem_o(i) + h0, o);
+        }
+    }
 }
 
 __device__ void output_role(const PagedParams& p, uint8_t* smem, Misc& ms, uint32_t tmem, int ow, int lane) {
@@ -1026,22 +1047,26 @@ __device__ void output_role(const PagedParams& p, uint8_t* smem, Misc& ms, uint3
         // a share's first unit, if it starts inside its row, is partial 0; the
         // part of a row that the share's end cuts off is partial 1
         float* part = p.part + static_cast<size_t>(2 * blockIdx.x + (flags & kInside ? 0 : 1)) * kPartialFloats;
+        bool deep = false;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int h = lane + 32 * e;
             const float l = empty ? 0.0f : (ms.red_l[0][h] + ms.red_l[1][h]) + (ms.red_l[2][h] + ms.red_l[3][h]);
             const float m = empty ? 0.0f : ms.m_ref[h];
             if (whole) {
-                ms.fac[ow][h] = h < p.H ? out_factor(m, l, p.sink, h) : 0.0f;
+                const float f = h < p.H ? out_factor(m, l, p.sink, h) : 0.0f;
+                ms.fac[ow][h] = f;
+                deep |= f < 0.0f;
             } else if (ow == 0) {
                 part[static_cast<size_t>(kHeadsPad) * kD + h] = m;
                 part[static_cast<size_t>(kHeadsPad) * kD + kHeadsPad + h] = l;
             }
         }
-        __syncwarp();
+        deep = __any_sync(0xffffffffu, deep);
         if (lane == 0) mbar_arrive(smem_addr(&ms.l_free));
         if (!paged_wait(smem_addr(&ms.o_full), nu & 1, ab, p.err)) return;
         tc_fence_after();
+        if (deep) deepen(ms.fac[ow], tmem + lane_off, 16 * (ow >> 2), p.H);
         const int d0 = 32 * qd + lane;
         // bf16: neighbouring lanes swap halves of (head j, head j + 1) pairs, so
         // that each stores two neighbouring columns of one head
@@ -1288,10 +1313,10 @@ __global__ void __launch_bounds__(128 * kMergeHeads) dsa_paged_combine_kernel(co
                 }
             }
         }
-        const float f = f_s[sub];
+        const float f = f_s[sub], pre = f < 0.0f ? kDeep : 1.0f;
         __nv_bfloat162* o2 = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + (static_cast<size_t>(row) * p.H + h) * kD) + 2 * col;
-        o2[0] = __floats2bfloat162_rn(acc.x * f, acc.y * f);
-        o2[1] = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+        o2[0] = __floats2bfloat162_rn(acc.x * pre * f, acc.y * pre * f);
+        o2[1] = __floats2bfloat162_rn(acc.z * pre * f, acc.w * pre * f);
     }
 }
 

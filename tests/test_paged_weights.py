@@ -177,6 +177,23 @@ def test_block_scales_far_apart_beside_a_flat_tail(S):
     _check(out[..., 4:], want[..., 4:], BIG + SMALL + BF16 + 2.2 * rel)
 
 
+@pytest.mark.parametrize("n,R", [(64, SHARES), (640, SHARES), (8192, SHARES), (32768, 3)])
+def test_heads_far_below_their_sink(n, R):
+    """Sinks of 0 to 98 above all scores: the outputs shrink with them, down to 1e-38, and no further off; whole rows
+    and cut ones."""
+    rng = np.random.default_rng(23)
+    H, sigma = 64, 2.0 ** -8
+    codes = _values(rng, n)
+    codes[:, 1] = ref.encode(np.clip(rng.standard_normal(n), -3.5, 3.5) * 64)
+    q = np.zeros((R, H, D))
+    q[..., 1] = 0.3 / (SCALE * LOG2E * sigma * 64.0)
+    out, want, rel = _run(codes, np.full(n // P, sigma), q, sink=np.linspace(0.0, 98.0, H))
+    # bf16 and float32 have numbers of 1.2e-38 and above to their full precision: heads of smaller outputs are left out
+    full = (want[..., 4:].amin(dim=(0, 2)) > 2.0 ** -125).nonzero()[:, 0]
+    assert 40 < len(full) < H
+    _check(out[:, full], want[:, full], TAIL + BF16 + 2.2 * rel)
+
+
 def test_a_long_tail_in_every_head_of_a_cut_row():
     """Three rows of 32768 keys, so that some fifty shares cut each: the parts' references differ by the dominant key
     (which one part holds) and the merge weighs them."""
