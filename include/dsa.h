@@ -353,8 +353,10 @@ DSA_API dsa_status dsa_qk_norm_rope(const void* q, const void* k, const float* q
  *   cache_scale [n_pages][page_size / scale_block] float32: one scale for
  *               each block of scale_block tokens of a page (the latent row is
  *               the cache's one key and value head).  A token's row is its
- *               codes times its block's scale; scales are positive, normal
- *               float32 numbers (the append writes powers of two).
+ *               codes times its block's scale; scales are positive float32
+ *               numbers from 2^-64 to 2^119 (the append writes powers of two,
+ *               and takes those of blocks that it adds to for such), those of
+ *               the keys of one row of an attention at most 2^90 apart.
  *   page_table  [B][max_pages] int32: position p of sequence b is token
  *               p % page_size of page page_table[b][p / page_size].  Only the
  *               entries of pages in use are read.
@@ -379,8 +381,9 @@ DSA_API dsa_status dsa_qk_norm_rope(const void* q, const void* k, const float* q
  * takes the new one and the codes held are rescaled to it (exactly, but for
  * codes that become subnormal, which round to nearest even).  Elements that
  * are not finite are stored as NaN and do not count in |y|.  Tokens before
- * seq_start[b] are taken as stored; tokens behind the last new one, and the
- * scales of blocks without a new token, stay as they were.
+ * seq_start[b] are taken as stored; codes behind the last new token, and the
+ * scales of blocks without a new token, stay as they were (a block's scale may
+ * change, so that what is stored behind its last new token has lost its value).
  * No two tokens of a call may have the same place in the cache, nor two
  * sequences tokens in the same block (a page shared by several sequences is
  * full before it is shared).  Repeating a call stores the same codes again.
@@ -420,7 +423,8 @@ DSA_API dsa_status dsa_paged_append(const void* kv, const float* norm_weight, fl
  * weights far below their head's largest, which may be further off or left out:
  * all they lose is at most 1.1 * 2^-7 of the sum of the row's weights, whatever
  * the row's length.  The denominator has all of them in float32.  An element of q
- * below 2^-15 of its head's largest may be off by 2^-23 of that largest.  A q
+ * below 2^-15 of its head's largest may be off by 2^-23 of that largest, or by
+ * 2^-122.  A q
  * element that is not finite makes its row and head NaN, and so does a NaN
  * code; a sink of NaN makes its head NaN, one of +inf zeros.  scale must be
  * finite.  Results do not depend on what other calls run, and repeated

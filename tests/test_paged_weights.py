@@ -177,6 +177,21 @@ def test_block_scales_far_apart_beside_a_flat_tail(S):
     _check(out[..., 4:], want[..., 4:], BIG + SMALL + BF16 + 2.2 * rel)
 
 
+@pytest.mark.parametrize("low,high", [(-64, 26), (29, 119)])
+@pytest.mark.parametrize("sink", [False, True])
+def test_scales_at_their_limits(low, high, sink):
+    """Blocks of the least and the greatest scales, 2^90 apart: q has nothing in their columns, so that all keys count
+    alike in the denominator, whatever their scale."""
+    rng = np.random.default_rng(19)
+    n, H = 1024, 8
+    codes = _values(rng, n)
+    scales = np.where(rng.random(n // 16) < 0.5, 2.0 ** low, 2.0 ** high)
+    q = np.zeros((SHARES, H, D))
+    q[..., 1] = rng.standard_normal((SHARES, H))
+    out, want, rel = _run(codes, scales, q, sink=np.linspace(0.0, 8.0, H) if sink else None)
+    _check(out, want, BIG + SMALL + BF16 + 2.2 * rel)
+
+
 @pytest.mark.parametrize("n,R", [(64, SHARES), (640, SHARES), (8192, SHARES), (32768, 3)])
 def test_heads_far_below_their_sink(n, R):
     """Sinks of 0 to 98 above all scores: the outputs shrink with them, down to 1e-38, and no further off; whole rows
