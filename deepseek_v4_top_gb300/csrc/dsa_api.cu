@@ -255,10 +255,10 @@ dsa_status run_paged(const void* q, const void* cache, const float* cache_scale,
     if (H > kHeadsPad) return DSA_ERR_UNSUPPORTED;
     if (!paged_sizes_ok(n_pages, page_size, scale_block, max_pages)) return DSA_ERR_INVALID_ARG;
     if (sparse && (k_max < 1 || k_max > kMaxKeys)) return DSA_ERR_INVALID_ARG;
-    if (static_cast<long long>(B) * T * H >= (1LL << 31)) return DSA_ERR_INVALID_ARG;
     // 32-bit tile counts
     const long long max_keys = sparse ? k_max : static_cast<long long>(max_pages) * page_size;
     if (static_cast<long long>(B) * T > (1LL << 30) / ((max_keys + 127) / 128)) return DSA_ERR_INVALID_ARG;
+    if (static_cast<long long>(B) * T * H >= (1LL << 31)) return DSA_ERR_INVALID_ARG;
     if (!isfinite(scale)) return DSA_ERR_INVALID_ARG;
     if (B == 0) return DSA_OK;
     if (!q || !cache || !cache_scale || !page_table || !seq_len || !out || !workspace) return DSA_ERR_INVALID_ARG;
