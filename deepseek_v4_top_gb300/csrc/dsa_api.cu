@@ -497,7 +497,6 @@ dsa_status dsa_paged_append(const void* kv, const float* norm_weight, float eps,
     p.R = R;
     p.B = B;
     p.n_pages = n_pages;
-    p.page_size = page_size;
     p.scale_block = scale_block;
     p.max_pages = max_pages;
     p.page_shift = dsa::log2_of(page_size);

@@ -118,7 +118,7 @@ struct AppendParams {
     uint32_t* err;
     float eps;                // < 0: no norm
     int n_positions, rope_dim;
-    int R, B, n_pages, page_size, scale_block, max_pages;
+    int R, B, n_pages, scale_block, max_pages;
     int page_shift, block_shift;
 };
 

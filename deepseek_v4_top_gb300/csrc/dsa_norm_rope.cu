@@ -93,7 +93,8 @@ __global__ void __launch_bounds__(kNrThreads) dsa_norm_rope_kernel(const NormRop
 
 cudaError_t launch_norm_rope(const NormRopeParams& params, bool bf16, bool halves, int sms, cudaStream_t s) {
     NormRopeParams p = params;
-    // enough blocks to fill every SM's warps; more rows loop
+    // more rows than these blocks have warps loop (three or four blocks of 256
+    // threads with 60 to 80 registers are resident on an SM at a time)
     const long long most = static_cast<long long>(sms) * 8;
     const long long qb = (static_cast<long long>(p.R) * p.H + kNrWarps - 1) / kNrWarps;
     const long long kb = (static_cast<long long>(p.R) * p.Hk + kNrWarps - 1) / kNrWarps;
