@@ -17,7 +17,7 @@
 //
 // What bounds it is latency: a CTA's chain of offsets, sequence, page and rows,
 // the norm's reductions, the block's maximum, the stores.  16384 rows of bf16 in
-// five sequences: 22 to 23 us (29 MB, 1.2 TB/s); 8 or 608 single tokens: 10 us,
+// five sequences: 23 to 26 us (29 MB, 1.2 TB/s); 8 or 608 single tokens: 10 us,
 // most of it the launch.  (Rows are on their way while the page is looked up: 1 us.)
 //
 // One CTA runs one group of G = max(8, scale_block) aligned positions of a

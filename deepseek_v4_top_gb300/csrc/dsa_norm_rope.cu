@@ -7,7 +7,7 @@
 // row, so the sum of squares is five shuffles and no shared memory.  What
 // limits it is how many bytes are on their way: a warp loads its next bf16 row
 // before it works on this one (2048 x 64 + 2048 heads of bf16, 273 MB: 50 ->
-// 45.5 us, 6.0 TB/s), while a float32 row has twice the bytes and the registers of a
+// 45.9 us, 6.0 TB/s), while a float32 row has twice the bytes and the registers of a
 // second one would cost warps (83 us without, 87 with it, for 545 MB).  More
 // warps with the weights reloaded for each row took 60 us and more.
 #include <math.h>

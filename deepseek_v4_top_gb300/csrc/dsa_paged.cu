@@ -26,7 +26,7 @@
 //     weight that would pass 2^8.75 (e4m3 ends at 448) moves the reference up.  A
 //     move rescales O in TMEM.  (With a largest weight of 1 at any length, one key 17
 //     octaves above 32767 flat ones lost a sixth of the output, and 2048 rows of 640
-//     keys took 256 us against 263 now; a first weight of 32 moves up in three tiles
+//     keys took 256 us against 262 now; a first weight of 32 moves up in three tiles
 //     of four, not in one of eight: 302 us with moves down by each tile's maxima.)
 //
 // Split: the rows' 128-key tiles, row after row, are cut into one equal share
@@ -36,13 +36,13 @@
 // within 1/8 of a share of a row's end moves there: a row more in one share
 // costs less than the two halves' partials, second start and merge.
 //
-// Measured (H = 64, one GB300): 8 rows of 32768 keys 72 us (135 MB, 1.9 TB/s); 608
-// rows of up to 640 selected keys 98 us (282 MB with q and out, 2.9 TB/s); 2048
-// rows of one sequence with 640 selected keys each 256 us (670 TFLOP/s of the
-// formulas' products); 8 rows of 640 keys 19 us with the merge.  What bounds it is
+// Measured (H = 64, one GB300): 8 rows of 32768 keys 73 us (135 MB, 1.9 TB/s); 608
+// rows of up to 640 selected keys 99 us (282 MB with q and out, 2.9 TB/s); 2048
+// rows of one sequence with 640 selected keys each 262 us (660 TFLOP/s of the
+// formulas' products); 8 rows of 640 keys 20 us with the merge.  What bounds it is
 // the chain of a tile, keys landed -> scores -> weights -> value product -> the
 // stage's next copy, with two tiles in flight: 5.5 to 6.5 thousand cycles a tile
-// against 3.2 of matrix instructions (tensor pipe 27 % busy, issue slots 42 %,
+// against 3.2 of matrix instructions (tensor pipe 25 % busy, issue slots 46 %,
 // DRAM under 30 %).  Leaving out all copies of keys, three quarters of the score
 // or of the value product, the later splits of Q, the moves or the stores of the
 // output shortens the 2048 rows by 2 to 10 % each, so no one of them is the
